@@ -46,6 +46,19 @@ mla_status_t mla_decode_attention_cudacore(const mla_bf16_t *q_full, const mla_b
 mla_status_t mla_debug_decode_wait(double wait_cap_seconds, int suppress_arrive);
 
 /*
+ * mla_debug_prefill_wait -- host. The same switch of the expanded attention's
+ * kernel (mla_prefill_attention) for the calls that follow.
+ *   wait_cap_seconds: how long nothing in a CTA may move on before a wait on a
+ *                     barrier gives up (default 1.0; must be > 0 and <= 10). Work
+ *                     that goes on is no reason, however long the call takes.
+ *   suppress_arrive:  1 = in each CTA the first zeroed tail of a sequence's values
+ *                     is not handed back, so the MMA issuer's wait for it can only
+ *                     end by running out; 0 = normal.
+ * Returns INVALID_ARGUMENT for a cap outside (0, 10].
+ */
+mla_status_t mla_debug_prefill_wait(double wait_cap_seconds, int suppress_arrive);
+
+/*
  * mla_debug_gemm_plan -- host, no device needed. The tile plan the
  * tensor-core GEMM takes for a problem, so that tests can check the planner
  * on the CPU. C[z][m][n] = sum_k A[z][m][k] B[z][n][k] with M weight rows, N

@@ -196,6 +196,7 @@ struct PrefillArgs {
   uint32_t *status;
 };
 mla_status_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
+mla_status_t set_prefill_wait(double seconds, int suppress_arrive);  // mla_debug_prefill_wait
 
 // The kernels behind each entry point (ops.cu).
 mla_status_t launch_absorb_q(const uint16_t *q_nope, int ld_qn, const uint16_t *q_pe, int ld_qp,

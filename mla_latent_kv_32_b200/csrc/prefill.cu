@@ -46,8 +46,11 @@
 // lies behind a sequence's keys never matters. A row that sees no key gets
 // o = 0 and lse = -inf.
 //
-// Every wait is bounded (about a second): on expiry MLA_DEV_TIMEOUT is set, the
-// CTA stops issuing, lets what it issued land and leaves.
+// Every wait is bounded: it gives up when nothing in the CTA has moved on for about
+// a second (each role counts the items it comes to, the MMA thread its steps too), so
+// the length of a call does not matter: the warp that zeroes tails may wait for its
+// first tile as long as the CTA works. On expiry MLA_DEV_TIMEOUT is set, the CTA stops
+// issuing, lets what it issued land and leaves.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -89,12 +92,12 @@ enum {
 };
 constexpr uint32_t kOffTmemPtr = kOffBar + 8 * B_COUNT;
 constexpr uint32_t kOffAbort = kOffTmemPtr + 4;
-constexpr uint32_t kOffSwap = (kOffAbort + 4 + 15) & ~15u;   // [stream][128] (maximum, sum)
+constexpr uint32_t kOffMoved = kOffAbort + 4;        // steps and items that the roles came to
+constexpr uint32_t kOffSwap = (kOffMoved + 4 + 15) & ~15u;   // [stream][128] (maximum, sum)
 constexpr uint32_t kSmemBytes = kOffSwap + 2 * 128 * 8;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 constexpr uint32_t kTmemS = 0, kTmemO = 256;         // stream i at + 128 i
-constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr float kRescale = 8.0f;                     // log2 units
 
 struct Args {
@@ -109,6 +112,8 @@ struct Args {
   long long ld_o, hs_o;
   float *lse;
   uint32_t *status;
+  uint64_t wait_ns;     // a wait gives up when nothing has moved for so long
+  int suppress_tail;    // test hook: the first tail is not handed back
 };
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
@@ -116,18 +121,27 @@ __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 struct Ctx {
   uint32_t bar_base;
   volatile int *abort_flag;
+  volatile int *moved;
   uint32_t *status;
+  uint64_t wait_ns;
   __device__ uint32_t bar(int i) const { return bar_base + 8u * i; }
+  // One thread of a role: it has come to its next item or step.
+  __device__ __forceinline__ void move() const { atomicAdd(const_cast<int *>(moved), 1); }
 };
 
 // (Inlined: a call would have to save the tile's scores around it.)
 __device__ __forceinline__ bool wait_slow(const Ctx &c, uint32_t bar, uint32_t parity, bool drain) {
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = globaltimer_ns();
+  int seen = *c.moved;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63) == 0) {
       if (!drain && *c.abort_flag) return false;
-      if (globaltimer_ns() - t0 > kTimeoutNs) {
+      const int now = *c.moved;
+      if (now != seen) {
+        seen = now;
+        t0 = globaltimer_ns();
+      } else if (globaltimer_ns() - t0 > c.wait_ns) {
         *c.abort_flag = 1;
         report(c.status, MLA_DEV_TIMEOUT);
         return false;
@@ -350,10 +364,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
   Ctx ctx;
   ctx.bar_base = base + kOffBar;
   ctx.abort_flag = reinterpret_cast<volatile int *>(smem + kOffAbort);
+  ctx.moved = reinterpret_cast<volatile int *>(smem + kOffMoved);
   ctx.status = a.status;
+  ctx.wait_ns = a.wait_ns;
   static_assert(B_COUNT <= 32, "a lane per barrier");
   if (warp == kTmaWarp) {
-    if (lane == 0) *ctx.abort_flag = 0;
+    if (lane == 0) *ctx.abort_flag = *ctx.moved = 0;
     if (lane < B_COUNT)
       mbar_init(ctx.bar(lane),
                 lane >= B_PFULL && lane < B_PFULL + 4 ? 4 : lane == B_SWAP ? 8 : 1);
@@ -422,6 +438,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
       bool turns = false;             // how the shared memory is laid out
       for (int i = i0; i < i1 && ok; ++i) {
         const Item it = load_item<kTurns>(a, items + i);
+        ctx.move();
         if (!it.ok) {
           report(a.status, MLA_DEV_BAD_PLAN);
           continue;
@@ -487,6 +504,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
       bool ok = true;
       for (int i = i0; i < i1 && ok; ++i) {
         const Item it = load_item<kTurns>(a, items + i);
+        ctx.move();
         if (!it.ok || it.tiles == 0) continue;
         const int n0 = it.count[0], n1 = it.count[1];   // no turns: n1 is 0 or >= n0
         const bool turns = kTurns && it.turns;
@@ -498,6 +516,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
 #pragma unroll 1
           for (int q = 0; q < 2 && ok; ++q) {
             const int count = q ? n1 : n0;
+            ctx.move();
             if (j >= 0 && j < count) {
               const int t = turns ? 2 * j + q : j;
               const uint32_t k = n + t;
@@ -573,6 +592,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
     uint32_t n = 0, tails = 0;
     for (int i = i0; i < i1; ++i) {
       const Item it = load_item<kTurns>(a, items + i);
+      if (lane == 0) ctx.move();
       if (!it.ok || it.tiles == 0) continue;
       const int t = it.tiles - 1;
       if (it.tail(t)) {
@@ -590,7 +610,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(ctx.bar(B_TAIL));
+        if (lane == 0 && !(a.suppress_tail && tails == 1)) mbar_arrive(ctx.bar(B_TAIL));
       }
       n += it.tiles;
     }
@@ -608,6 +628,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
     bool ok = true, unread = false;
     for (int i = i0; i < i1 && ok; ++i) {
       const Item it = load_item<kTurns>(a, items + i);
+      if (lane == 0) ctx.move();
       if (!it.ok) continue;
       const int row = lrow + (kTurns && it.turns ? 0 : 128 * q);   // of the item
       const bool has = row < it.q_rows;
@@ -870,6 +891,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_combine_kernel(const
 
 }  // namespace
 
+// failure-detection switch (mla_debug_prefill_wait)
+static uint64_t g_wait_ns = 1000000000ull;
+static int g_suppress_tail = 0;
+
+mla_status_t set_prefill_wait(double seconds, int suppress_arrive) {
+  if (!(seconds > 0.0 && seconds <= 10.0))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "wait cap %g s outside (0, 10]", seconds);
+  g_wait_ns = (uint64_t)(seconds * 1e9);
+  g_suppress_tail = suppress_arrive ? 1 : 0;
+  return MLA_OK;
+}
+
 mla_status_t launch_prefill(const PrefillArgs &p, cudaStream_t stream) {
   const PrefillHeader *ph = p.plan_host;
   CUtensorMap qn, qp, kn, v, kp;
@@ -905,6 +938,8 @@ mla_status_t launch_prefill(const PrefillArgs &p, cudaStream_t stream) {
   a.hs_o = p.hs_o;
   a.lse = p.lse;
   a.status = p.status;
+  a.wait_ns = g_wait_ns;
+  a.suppress_tail = g_suppress_tail;
   auto kernel = ph->turns ? prefill_kernel<true> : prefill_kernel<false>;
   MLA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kSmemBytes));

@@ -68,6 +68,7 @@ SIGNATURES = {
     "mla_decode_attention": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _P,
                                   _P, _P]),
     "mla_debug_decode_wait": (_I, [ctypes.c_double, _I]),
+    "mla_debug_prefill_wait": (_I, [ctypes.c_double, _I]),
     "mla_debug_gemm_plan": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "mla_decode_attention_cudacore": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _SZ,
                                            _P, _P, _P, _P]),
@@ -232,6 +233,12 @@ def mla_debug_decode_wait(wait_cap_seconds: float = 1.0, suppress_arrive: int = 
     """Failure-detection switch of the tensor-core decode kernel (include/mla_debug.h)."""
     _check(load().mla_debug_decode_wait(float(wait_cap_seconds), int(suppress_arrive)),
            "mla_debug_decode_wait")
+
+
+def mla_debug_prefill_wait(wait_cap_seconds: float = 1.0, suppress_arrive: int = 0):
+    """Failure-detection switch of the expanded attention's kernel (include/mla_debug.h)."""
+    _check(load().mla_debug_prefill_wait(float(wait_cap_seconds), int(suppress_arrive)),
+           "mla_debug_prefill_wait")
 
 
 def mla_debug_gemm_plan(M, N, K, batch=1, a_mn=0, c_fp32=0, fp32_part=0, atomic_split=0,

@@ -527,9 +527,14 @@ mla_status_t launch_gemm_tc(const GemmTcDesc &d, cudaStream_t stream) {
     MLA_CUDA_TRY(cudaMemsetAsync(d.split_ws, 0, (size_t)d.M * d.N * d.batch * sizeof(float),
                                  stream));
   } else if (splits > 1 && !pl.part) {
-    if (!d.c_contiguous)
-      return fail(MLA_ERR_UNSUPPORTED, "split-K needs a contiguous fp32 output");
-    MLA_CUDA_TRY(cudaMemsetAsync(d.C, 0, d.c_bytes, stream));
+    if (d.batch != 1 || d.sCm != 1)
+      return fail(MLA_ERR_UNSUPPORTED, "split-K needs an fp32 output with contiguous rows");
+    // rows of M floats at a stride of sCn: what lies between them is the caller's
+    const size_t row = (size_t)d.M * sizeof(float);
+    if (d.sCn == d.M)
+      MLA_CUDA_TRY(cudaMemsetAsync(d.C, 0, row * d.N, stream));
+    else
+      MLA_CUDA_TRY(cudaMemset2DAsync(d.C, (size_t)d.sCn * sizeof(float), 0, row, d.N, stream));
   }
   auto kernel = d.row_c ? gemm_tc_kernel<false, true>
                 : two_m ? gemm_tc_kernel<true, false> : gemm_tc_kernel<false, false>;

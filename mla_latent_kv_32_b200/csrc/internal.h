@@ -41,10 +41,8 @@ struct GemmTcDesc {
   long long sCz, sCm, sCn;
   int c_fp32;
   int M, N, K, batch;
-  int allow_split;       // fp32 output may be split over K (atomic adds, zeroed first)
+  int allow_split;       // fp32 output may be split over K (atomic adds, zeroed first: batch 1, sCm 1)
   int row_c;             // sCn == 1, bf16, no split, N % 8 == 0, C rows 16-byte aligned: wide stores
-  int c_contiguous;      // C occupies c_bytes contiguous bytes (needed for the split)
-  size_t c_bytes;
   uint32_t *status;
   // bf16 output with a split over K: fp32 partial sums accumulate in
   // split_ws (M*N*batch floats, element (z, n, m) at (z*N + n)*M + m), then

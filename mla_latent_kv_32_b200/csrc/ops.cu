@@ -62,8 +62,6 @@ mla_status_t launch_projection(const uint16_t *X, int ld_x, const uint16_t *W, i
   d.C = C; d.sCz = 0; d.sCm = 1; d.sCn = ld_c;
   d.c_fp32 = c_fp32; d.M = N; d.N = M; d.K = K; d.batch = 1;
   d.allow_split = c_fp32;
-  d.c_contiguous = 1;
-  d.c_bytes = (size_t)M * ld_c * (c_fp32 ? 4 : 2);
   d.split_ws = c_fp32 ? nullptr : ws;
   d.part_ws = c_fp32 ? ws : nullptr;
   d.part_ws_bytes = c_fp32 ? ws_bytes : 0;

@@ -1,0 +1,52 @@
+"""mla_gemm_bf16 into a column slice of a wider buffer: what lies beside the slice,
+before and behind it, stays as it was, whatever way the product is split.
+
+Tolerance: products of bf16 values are exact in float32; K additions, each off by
+at most 2^-24 of a partial sum, so K 2^-24 sum |x w| (a bf16 output: 2^-8 of the
+value more)."""
+
+import pytest
+import torch
+
+from mla_latent_kv_32_b200 import build as build_mod
+from mla_latent_kv_32_b200 import mla
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build_mod.build()
+    mla.load()
+    return torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("workspace", [False, True])
+@pytest.mark.parametrize("fp32", [1, 0])
+@pytest.mark.parametrize("m,n,k", [(4, 64, 2048), (1, 8, 1024), (64, 136, 7168), (129, 520, 4096),
+                                   (300, 2112, 512)])
+def test_gemm_into_a_column_slice(dev, m, n, k, fp32, workspace):
+    g = torch.Generator().manual_seed(m + n)
+    x = torch.randn(m, k, generator=g).to(torch.bfloat16)
+    w = torch.randn(n, k, generator=g).to(torch.bfloat16)
+    left, right = 64, 40
+    ld = left + n + right
+    # two rows behind the last, so that no write leaves the buffer unseen
+    buf = torch.full((m + 2, ld), 7.0, dtype=torch.float32 if fp32 else torch.bfloat16, device=dev)
+    need = mla.mla_gemm_bf16_workspace_bytes(m, n, k) if workspace else 0
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    xd, wd = x.to(dev), w.to(dev)
+    for _ in range(2):    # again over its own result
+        mla.mla_gemm_bf16_ws(xd, k, wd, k, buf[:, left:], ld, fp32, m, n, k,
+                             ws if workspace else None, need)
+    torch.cuda.synchronize()
+    out = buf.cpu()
+    got = out[:m, left:left + n].double().clone()
+    out[:m, left:left + n] = 7.0
+    assert (out == 7.0).all()
+    x, w = x.double(), w.double()
+    want = x @ w.T
+    tol = k * 2.0 ** -24 * (x.abs() @ w.abs().T) + (0 if fp32 else 2.0 ** -8) * want.abs()
+    assert ((got - want).abs() <= tol).all()

@@ -574,10 +574,14 @@ mla_status_t mla_cache_gather_fp8(const uint8_t *cache, const float *scales, int
  *           0: every key of the sequence.
  *   num_ctas:  work lists; 0 = one per SM of the current device.
  *   max_split: 1 = no (query tile, head) is split over its keys; 0 = split where
- *              possible; negative = by the smaller estimated time.
- *   plan: host buffer of mla_prefill_plan_bytes(q_lens, batch, n_h, num_ctas).
+ *              possible (as any value above 1); negative = by the smaller
+ *              estimated time.
+ *   plan: host buffer of mla_prefill_plan_bytes(q_lens, batch, n_h, num_ctas),
+ *         which is 0 where no plan can be made: a negative length or n_h < 1, or a
+ *         plan of 2^31 bytes or more.
  * One plan serves every layer of the step. Copy it to the device with
- * mla_plan_upload. Supported: 1 <= n_h <= 128.
+ * mla_plan_upload. Supported: 1 <= n_h <= 128, at most 2^31 - 1 query rows and as
+ * many keys in all, a plan below 2^31 bytes.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE_TOO_SMALL (plan buffer).
  */
 size_t mla_prefill_plan_bytes(const int32_t *q_lens, int batch, int n_h, int num_ctas);

@@ -85,7 +85,7 @@ long long prefill_units(const int32_t *q_lens, int batch, int n_h) {
   long long tiles = 0;
   for (int b = 0; b < batch; ++b) {
     if (q_lens[b] < 0) return -1;
-    tiles += (q_lens[b] + kPrefillRows - 1) / kPrefillRows;
+    tiles += ((long long)q_lens[b] + kPrefillRows - 1) / kPrefillRows;
   }
   return tiles * n_h;
 }
@@ -479,7 +479,8 @@ size_t mla_prefill_plan_bytes(const int32_t *q_lens, int batch, int n_h, int num
   if (batch < 0 || n_h < 1 || (batch > 0 && q_lens == nullptr)) return 0;
   if (prefill_ctas(&num_ctas) != MLA_OK) return 0;
   const long long units = prefill_units(q_lens, batch, n_h);
-  return units < 0 ? 0 : prefill_bytes(units, num_ctas);
+  const size_t need = units < 0 ? 0 : prefill_bytes(units, num_ctas);
+  return need > INT_MAX ? 0 : need;
 }
 
 mla_status_t mla_prefill_plan(const int32_t *q_lens, const int32_t *kv_lens, int batch, int n_h,

@@ -76,6 +76,19 @@ mla_status_t mla_debug_prefill_wait(double wait_cap_seconds, int suppress_arrive
 mla_status_t mla_debug_gemm_plan(int M, int N, int K, int batch, int a_mn, int c_fp32,
                                  int fp32_part, int atomic_split, int sms, int32_t *out);
 
+/*
+ * mla_debug_projection_plan -- host, no device needed. What mla_gemm_bf16 (workspace
+ * 0) or mla_gemm_bf16_ws (1) launches for M tokens, N features and a reduction K: the
+ * weights on the kernel's M side and the tokens on its N side, or, where bf16 outputs
+ * of a short reduction are stored by rows, the other way round.
+ *   out[0..7] as mla_debug_gemm_plan's, of the sides as launched,
+ *   out[8] 1 when the tokens are the kernel's M side,
+ *   out[9] k-chunks in flight per CTA.
+ * Returns INVALID_ARGUMENT for non-positive sizes or a NULL `out`.
+ */
+mla_status_t mla_debug_projection_plan(int M, int N, int K, int c_fp32, int workspace, int sms,
+                                       int32_t *out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -578,13 +578,7 @@ mla_status_t mla_cache_append_fp8(uint8_t *cache, float *scales, int num_pages,
                                  status, (cudaStream_t)stream);
 }
 
-mla_status_t mla_debug_gemm_plan(int M, int N, int K, int batch, int a_mn, int c_fp32,
-                                 int fp32_part, int atomic_split, int sms, int32_t *out) {
-  clear_error();
-  MLA_CHECK_ARG(out != nullptr, "NULL out");
-  MLA_CHECK_ARG(M > 0 && N > 0 && K > 0 && batch > 0 && sms > 0, "non-positive size");
-  const GemmPlan pl = plan_gemm(M, N, K, batch, a_mn != 0, c_fp32 != 0, fp32_part != 0,
-                                atomic_split != 0, sms);
+static void write_gemm_plan(const GemmPlan &pl, int32_t *out) {
   out[0] = pl.BN;
   out[1] = pl.two_m ? 2 : 1;
   out[2] = pl.ntile;
@@ -593,6 +587,31 @@ mla_status_t mla_debug_gemm_plan(int M, int N, int K, int batch, int a_mn, int c
   out[5] = pl.k_chunks;
   out[6] = pl.part ? 1 : 0;
   out[7] = (int32_t)std::min<size_t>(pl.part_bytes, 0x7FFFFFFF);
+}
+
+mla_status_t mla_debug_gemm_plan(int M, int N, int K, int batch, int a_mn, int c_fp32,
+                                 int fp32_part, int atomic_split, int sms, int32_t *out) {
+  clear_error();
+  MLA_CHECK_ARG(out != nullptr, "NULL out");
+  MLA_CHECK_ARG(M > 0 && N > 0 && K > 0 && batch > 0 && sms > 0, "non-positive size");
+  write_gemm_plan(plan_gemm(M, N, K, batch, a_mn != 0, c_fp32 != 0, fp32_part != 0,
+                            atomic_split != 0, false, sms),
+                  out);
+  return MLA_OK;
+}
+
+mla_status_t mla_debug_projection_plan(int M, int N, int K, int c_fp32, int workspace, int sms,
+                                       int32_t *out) {
+  clear_error();
+  MLA_CHECK_ARG(out != nullptr, "NULL out");
+  MLA_CHECK_ARG(M > 0 && N > 0 && K > 0 && sms > 0, "non-positive size");
+  const bool f32 = c_fp32 != 0, ws = workspace != 0;
+  const bool rows = projection_by_rows(M, N, K, f32, ws);
+  const GemmPlan pl = rows ? plan_gemm(M, N, K, 1, false, false, false, false, true, sms)
+                           : plan_gemm(N, M, K, 1, false, f32, f32 && ws, f32 || ws, false, sms);
+  write_gemm_plan(pl, out);
+  out[8] = rows ? 1 : 0;
+  out[9] = pl.stages;
   return MLA_OK;
 }
 
@@ -634,7 +653,8 @@ size_t mla_gemm_bf16_workspace_bytes(int M, int N, int K) {
   const size_t bf16_need = ((size_t)M * N * sizeof(float) + 255) & ~(size_t)255;
   int sms = 0;
   if (device_info(&sms, nullptr, nullptr) != MLA_OK) return bf16_need;
-  return std::max(bf16_need, plan_gemm(N, M, K, 1, false, true, true, false, sms).part_bytes);
+  return std::max(bf16_need,
+                  plan_gemm(N, M, K, 1, false, true, true, false, false, sms).part_bytes);
 }
 
 mla_status_t mla_gemm_bf16_ws(const mla_bf16_t *X, int ld_x, const mla_bf16_t *W, int ld_w,

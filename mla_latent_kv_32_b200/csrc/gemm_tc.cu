@@ -43,6 +43,7 @@ constexpr int kMaxStages = 8;          // ring depth when one CTA per SM covers 
 constexpr int kSharedStages = 4;       // ring depth when CTAs share SMs
 constexpr uint32_t kSmemLimit = 232448;  // dynamic shared memory per CTA (227 KB)
 constexpr uint32_t kAStage = 128 * 128;        // 128 rows x 64 k (bf16) = 16 KB
+constexpr uint32_t kBarBytes = 8 * (2 * kMaxStages + 2);
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr int kMaxPartSplits = 8;      // fp32 split-K into partial-sum tiles: at most this many
 
@@ -395,8 +396,13 @@ mla_status_t make_map3(CUtensorMap_st *tm, const void *ptr, uint64_t d0, uint64_
   return MLA_OK;
 }
 
+// A k-chunk of a tile: 128 (or 256) rows of A and BN of B, whole kilobytes.
+static uint32_t stage_bytes(const GemmPlan &pl) {
+  return (pl.two_m ? 2 : 1) * kAStage + (((uint32_t)pl.BN * 128 + 1023u) & ~1023u);
+}
+
 GemmPlan plan_gemm(int M, int N, int K, int batch, bool a_mn, bool c_fp32, bool fp32_part,
-                   bool atomic_split, int sms) {
+                   bool atomic_split, bool row_c, int sms) {
   GemmPlan pl;
   pl.BN = N >= 256 ? 256 : ((N + 15) / 16) * 16;
   pl.ntile = (N + pl.BN - 1) / pl.BN;
@@ -432,9 +438,24 @@ GemmPlan plan_gemm(int M, int N, int K, int batch, bool a_mn, bool c_fp32, bool 
     pl.two_m = big_m && pl.splits == 1;
     pl.mtile = (M + (pl.two_m ? 255 : 127)) / (pl.two_m ? 256 : 128);
   }
+  if (row_c) {
+    // one accumulator and two stages, so that two CTAs share an SM and one's
+    // stores run beside the other's MMAs
+    pl.two_m = 0;
+    pl.mtile = (M + 127) / 128;
+  }
   pl.k_chunks = (kchunks + pl.splits - 1) / pl.splits;
   pl.part_bytes =
       pl.part ? ((size_t)pl.splits * M * N * batch * sizeof(float) + 255) & ~(size_t)255 : 0;
+  // A grid that fits one CTA per SM keeps every k-chunk of a tile in flight
+  // (up to kMaxStages, within the shared memory), so a tile waits one load
+  // round trip rather than one per ring cycle; denser grids keep a shallower
+  // ring and several CTAs per SM.
+  const int fit = (int)((kSmemLimit - 1024 - kBarBytes) / stage_bytes(pl));
+  const long long tile_ctas = (long long)pl.ntile * pl.mtile * batch * pl.splits;
+  const int depth = row_c ? 2 : tile_ctas <= sms ? std::min(kMaxStages, fit)
+                                                 : std::min(kSharedStages, fit);
+  pl.stages = std::min(pl.k_chunks, depth);
   return pl;
 }
 
@@ -461,40 +482,25 @@ mla_status_t launch_gemm_tc(const GemmTcDesc &d, cudaStream_t stream) {
   int sms = 0;
   st = device_info(&sms, nullptr, nullptr);
   if (st != MLA_OK) return st;
-  GemmPlan pl = plan_gemm(d.M, d.N, d.K, d.batch, d.a_mn, d.c_fp32 != 0,
-                          d.c_fp32 && d.part_ws != nullptr,
-                          (d.c_fp32 && d.allow_split) || (!d.c_fp32 && d.split_ws != nullptr), sms);
-  if (d.row_c) {
-    // one accumulator and two stages, so that two CTAs share an SM and one's
-    // stores run beside the other's MMAs
-    pl.two_m = 0;
-    pl.mtile = (d.M + 127) / 128;
-  }
+  const GemmPlan pl = plan_gemm(d.M, d.N, d.K, d.batch, d.a_mn, d.c_fp32 != 0,
+                                d.c_fp32 && d.part_ws != nullptr,
+                                (d.c_fp32 && d.allow_split) || (!d.c_fp32 && d.split_ws != nullptr),
+                                d.row_c != 0, sms);
   if (pl.part && d.part_ws_bytes < pl.part_bytes)
     return fail(MLA_ERR_WORKSPACE_TOO_SMALL, "GEMM workspace %zu B < %zu B", d.part_ws_bytes,
                 pl.part_bytes);
-  const int kchunks = (d.K + 63) / 64;
   const bool two_m = pl.two_m;
   const int ntile = pl.ntile, mtile = pl.mtile;
   const int splits = pl.splits;
   const bool ws_split = splits > 1 && !d.c_fp32;
   g.part = pl.part ? d.part_ws : nullptr;
   g.splits = splits;
-  g.k_chunks = (kchunks + splits - 1) / splits;
-  g.stage_bytes = (two_m ? 2 : 1) * kAStage + (((uint32_t)BN * 128 + 1023u) & ~1023u);
-  // A grid that fits one CTA per SM keeps every k-chunk of a tile in flight
-  // (up to kMaxStages, within the shared memory), so a tile waits one load
-  // round trip rather than one per ring cycle; denser grids keep a shallower
-  // ring and several CTAs per SM.
-  const uint32_t bar_bytes = 8 * (2 * kMaxStages + 2);
-  const int fit = (int)((kSmemLimit - 1024 - bar_bytes) / g.stage_bytes);
-  const long long tile_ctas = (long long)ntile * mtile * d.batch * splits;
-  const int depth = d.row_c ? 2 : tile_ctas <= sms ? std::min(kMaxStages, fit)
-                                                  : std::min(kSharedStages, fit);
-  g.stages = std::min(g.k_chunks, depth);
+  g.k_chunks = pl.k_chunks;
+  g.stage_bytes = stage_bytes(pl);
+  g.stages = pl.stages;
   g.tmem_cols = 32;
   while (g.tmem_cols < (uint32_t)(two_m ? 2 * BN : BN)) g.tmem_cols *= 2;
-  const uint32_t smem_bytes = g.stages * g.stage_bytes + bar_bytes + 1024;
+  const uint32_t smem_bytes = g.stages * g.stage_bytes + kBarBytes + 1024;
   g.batch = d.batch;
   g.a_mn = d.a_mn;
   g.C = d.C;

@@ -76,11 +76,16 @@ mla_status_t make_map3(CUtensorMap_st *tm, const void *ptr, uint64_t d0, uint64_
 // Tile shape and K split launch_gemm_tc takes for a problem (gemm_tc.cu).
 struct GemmPlan {
   int BN, two_m, ntile, mtile, splits, k_chunks;
+  int stages;         // depth of a CTA's ring of k-chunks
   bool part;          // fp32 partial-sum tiles in a workspace
   size_t part_bytes;  // the workspace those need
 };
 GemmPlan plan_gemm(int M, int N, int K, int batch, bool a_mn, bool c_fp32, bool fp32_part,
-                   bool atomic_split, int sms);
+                   bool atomic_split, bool row_c, int sms);
+
+// Whether launch_projection puts the tokens on the M side (row_c), M tokens, N features
+// (ops.cu).
+bool projection_by_rows(int M, int N, int K, bool c_fp32, bool workspace);
 
 mla_status_t launch_cache_append(uint16_t *cache, int num_pages, const int32_t *block_table,
                                  int batch, int max_pages, const int32_t *seq_idx,

@@ -37,19 +37,23 @@ mla_status_t launch_out_absorb(const uint16_t *o_latent, const uint16_t *w_uv, i
 constexpr int kManyTokens = 64, kShortK = 2048;
 constexpr int kGridTokens = 65535 * 128;   // tokens on the grid's y axis
 
+// A short reduction, where the stores of C are most of the time: the tokens are
+// the M side and a thread's output row is contiguous (wide stores). The same
+// bits; 16384 tokens x 16384 x 512: 313 us against 1031 the other way round, 256
+// x 16384 x 512: 12 against 41; but 4096 x 7168 x 16384: 888 against 815 (with
+// 16-byte stores, 10 % slower on the short ones). (Fewer than 64 tokens fill
+// little of a tile's 128 rows and stay on the N side.)
+bool projection_by_rows(int M, int N, int K, bool c_fp32, bool workspace) {
+  return !c_fp32 && !workspace && M >= kManyTokens && M <= kGridTokens && K <= kShortK &&
+         N % 8 == 0;
+}
+
 // C[t][f] = sum_k X[t][k] * W[f][k]   (m = output feature f, n = token t)
 mla_status_t launch_projection(const uint16_t *X, int ld_x, const uint16_t *W, int ld_w, void *C,
                                int ld_c, int c_fp32, int M, int N, int K, float *ws,
                                size_t ws_bytes, cudaStream_t stream) {
   GemmTcDesc d = {};
-  // A short reduction, where the stores of C are most of the time: the tokens are
-  // the M side and a thread's output row is contiguous (wide stores). The same
-  // bits; 16384 tokens x 16384 x 512: 313 us against 1031 the other way round, 256
-  // x 16384 x 512: 12 against 41; but 4096 x 7168 x 16384: 888 against 815 (with
-  // 16-byte stores, 10 % slower on the short ones). (Fewer than 64 tokens fill
-  // little of a tile's 128 rows and stay on the N side.)
-  if (!c_fp32 && ws == nullptr && M >= kManyTokens && M <= kGridTokens && K <= kShortK &&
-      N % 8 == 0) {
+  if (projection_by_rows(M, N, K, c_fp32 != 0, ws != nullptr)) {
     d.A = X; d.sAm = ld_x;
     d.B = W; d.sBn = ld_w;
     d.C = C; d.sCm = ld_c; d.sCn = 1;

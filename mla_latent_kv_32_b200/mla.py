@@ -70,6 +70,7 @@ SIGNATURES = {
     "mla_debug_decode_wait": (_I, [ctypes.c_double, _I]),
     "mla_debug_prefill_wait": (_I, [ctypes.c_double, _I]),
     "mla_debug_gemm_plan": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "mla_debug_projection_plan": (_I, [_I, _I, _I, _I, _I, _I, _P]),
     "mla_decode_attention_cudacore": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _SZ,
                                            _P, _P, _P, _P]),
     "mla_decode_attention_noalloc": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P,
@@ -241,14 +242,24 @@ def mla_debug_prefill_wait(wait_cap_seconds: float = 1.0, suppress_arrive: int =
            "mla_debug_prefill_wait")
 
 
+_GEMM_PLAN = ("BN", "accumulators", "ntile", "mtile", "splits", "k_chunks", "part", "part_bytes")
+
+
 def mla_debug_gemm_plan(M, N, K, batch=1, a_mn=0, c_fp32=0, fp32_part=0, atomic_split=0,
                         sms=148) -> dict:
     """The tensor-core GEMM's tile plan for a problem (include/mla_debug.h)."""
     out = (ctypes.c_int32 * 8)()
     _check(load().mla_debug_gemm_plan(M, N, K, batch, int(a_mn), int(c_fp32), int(fp32_part),
                                       int(atomic_split), sms, out), "mla_debug_gemm_plan")
-    keys = ("BN", "accumulators", "ntile", "mtile", "splits", "k_chunks", "part", "part_bytes")
-    return dict(zip(keys, list(out)))
+    return dict(zip(_GEMM_PLAN, list(out)))
+
+
+def mla_debug_projection_plan(M, N, K, c_fp32=0, workspace=0, sms=148) -> dict:
+    """What mla_gemm_bf16[_ws] launches for a projection (include/mla_debug.h)."""
+    out = (ctypes.c_int32 * 10)()
+    _check(load().mla_debug_projection_plan(M, N, K, int(c_fp32), int(workspace), sms, out),
+           "mla_debug_projection_plan")
+    return dict(zip(_GEMM_PLAN + ("tokens_on_m", "stages"), list(out)))
 
 
 def mla_decode_attention_cudacore(q_full, cache, num_pages, block_table, max_pages, batch, q_len,

@@ -439,8 +439,8 @@ GemmPlan plan_gemm(int M, int N, int K, int batch, bool a_mn, bool c_fp32, bool 
     pl.mtile = (M + (pl.two_m ? 255 : 127)) / (pl.two_m ? 256 : 128);
   }
   if (row_c) {
-    // one accumulator and two stages, so that two CTAs share an SM and one's
-    // stores run beside the other's MMAs
+    // one accumulator, so that two CTAs can share an SM and one's stores run beside
+    // the other's MMAs
     pl.two_m = 0;
     pl.mtile = (M + 127) / 128;
   }
@@ -450,11 +450,14 @@ GemmPlan plan_gemm(int M, int N, int K, int batch, bool a_mn, bool c_fp32, bool 
   // A grid that fits one CTA per SM keeps every k-chunk of a tile in flight
   // (up to kMaxStages, within the shared memory), so a tile waits one load
   // round trip rather than one per ring cycle; denser grids keep a shallower
-  // ring and several CTAs per SM.
+  // ring and several CTAs per SM (two stages where rows are stored: two CTAs).
+  // Rows with two stages on a small grid, weights out of HBM: 64 tokens x 512 x
+  // 2048 27.5 us instead of 17.6, 256 x 7168 x 1536 23.1 instead of 15.8.
   const int fit = (int)((kSmemLimit - 1024 - kBarBytes) / stage_bytes(pl));
   const long long tile_ctas = (long long)pl.ntile * pl.mtile * batch * pl.splits;
-  const int depth = row_c ? 2 : tile_ctas <= sms ? std::min(kMaxStages, fit)
-                                                 : std::min(kSharedStages, fit);
+  const int depth = tile_ctas <= sms ? std::min(kMaxStages, fit)
+                    : row_c          ? 2
+                                     : std::min(kSharedStages, fit);
   pl.stages = std::min(pl.k_chunks, depth);
   return pl;
 }

@@ -50,3 +50,15 @@ def test_projection_plan_refusals():
         with pytest.raises(mla.MlaError) as e:
             mla.mla_debug_projection_plan(*args)
         assert e.value.status == mla.MLA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 512, 2048), (128, 512, 2048), (256, 512, 2048),
+                                   (64, 24576, 2048), (256, 7168, 1536), (64, 64, 512)])
+def test_a_grid_below_one_wave_keeps_a_deep_ring(M, N, K):
+    # a CTA alone on its SM has nothing else to hide its loads behind
+    p = mla.mla_debug_projection_plan(M, N, K, 0, 0, SMS)
+    assert p["tokens_on_m"] and p["ntile"] * p["mtile"] <= SMS
+    stage = 16384 + p["BN"] * 128
+    assert p["stages"] == min(8, p["k_chunks"], (232448 - 2048) // stage) >= 4
+    dense = mla.mla_debug_projection_plan(4096, 16384, 512, 0, 0, SMS)
+    assert dense["stages"] == 2

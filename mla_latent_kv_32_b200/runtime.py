@@ -70,7 +70,7 @@ class DecodeSession(_GraphStep):
 
     def __init__(self, inp, device="cuda", num_ctas: int = 0, max_split: int = -1,
                  scale: float = DEFAULT_SCALE, rope_table: Optional[np.ndarray] = None,
-                 fp8: bool = False):
+                 fp8: bool = False, prefix_layout: int = mla.MLA_ROPE_INTERLEAVED):
         w = inp.w
         self.w = w
         self.fp8 = fp8
@@ -108,14 +108,15 @@ class DecodeSession(_GraphStep):
         self.u = torch.empty((self.T, self.n_h * D_V), dtype=torch.bfloat16, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         if fp8:
-            self._fp8_pool(inp)
+            self._fp8_pool(inp, prefix_layout)
 
-    def _fp8_pool(self, inp):
+    def _fp8_pool(self, inp, layout):
         """The FP8 cache of this workload: every slot starts as a large
         finite filler (latent code 128.0, scale 1, k^R bf16 64.0); the
         workload's prefix rows [c | k] then enter through the library's own
         FP8 append at their positions (k rotated there), as a prefill would
-        write them. The bf16 pool is dropped."""
+        write them (in the half layout: as the interleaved pairs that
+        append turns, put back in their places). The bf16 pool is dropped."""
         dev = self.device
         self.cache = None
         self.cache8 = torch.empty((self.num_pages, PAGE, FP8_ROW), dtype=torch.uint8, device=dev)
@@ -134,10 +135,16 @@ class DecodeSession(_GraphStep):
             pos.append(np.arange(n, dtype=np.int32))
         if rows:
             r = to_dev_bf16(np.concatenate(rows), dev)
+            half = layout == mla.MLA_ROPE_HALF
+            if half:
+                r[:, D_C:] = r[:, D_C:].view(-1, 2, D_R // 2).transpose(1, 2).reshape(-1, D_R)
             sq, ps = to_dev(np.concatenate(seq), dev), to_dev(np.concatenate(pos), dev)
             mla.mla_cache_append_fp8(self.cache8, self.scales8, self.num_pages, self.table, self.B,
                                      self.max_pages, sq, ps, r, ROW, r[:, D_C:], ROW, self.rope,
                                      self.max_pos, r.shape[0], self.status)
+            if half:     # (the filler is one value)
+                k = self.cache8[:, :, D_C:].view(torch.bfloat16)
+                k.copy_(k.view(*k.shape[:2], D_R // 2, 2).transpose(2, 3).reshape(k.shape))
             torch.cuda.synchronize(dev)
             del r, sq, ps
 
@@ -240,7 +247,7 @@ class PrefillSession(_GraphStep):
             raise ValueError("the plain append takes the interleaved layout only")
         # the decode step's buffers that a chunk shares: cache, table, weights, new rows
         self.base = DecodeSession(inp, device, max_split=1, scale=scale, rope_table=rope_table,
-                                  fp8=fp8)
+                                  fp8=fp8, prefix_layout=layout)
         b, dev, n_h = self.base, self.base.device, self.base.n_h
         self.w, self.device, self.fp8, self.scale, self.layout = w, dev, fp8, scale, layout
         self.B, self.n_h, self.status = b.B, n_h, b.status

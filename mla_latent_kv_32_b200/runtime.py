@@ -70,7 +70,8 @@ class DecodeSession(_GraphStep):
 
     def __init__(self, inp, device="cuda", num_ctas: int = 0, max_split: int = -1,
                  scale: float = DEFAULT_SCALE, rope_table: Optional[np.ndarray] = None,
-                 fp8: bool = False, prefix_layout: int = mla.MLA_ROPE_INTERLEAVED):
+                 fp8: bool = False, prefix_layout: int = mla.MLA_ROPE_INTERLEAVED,
+                 decode: bool = True):
         w = inp.w
         self.w = w
         self.fp8 = fp8
@@ -96,7 +97,16 @@ class DecodeSession(_GraphStep):
         self.max_pos = int(inp.lens.max()) if rope_table is None else rope_table.shape[0]
         tab = mla.mla_rope_table(self.max_pos) if rope_table is None else rope_table
         self.rope = to_dev(tab, dev)
-        self.plan_host, self.info = mla.mla_decode_plan(inp.lens, self.B, self.q_len, self.n_h,
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        if decode:
+            self._decode_buffers(num_ctas, max_split)
+        if fp8:
+            self._fp8_pool(inp, prefix_layout)
+
+    def _decode_buffers(self, num_ctas, max_split):
+        """The plan, workspace and outputs of the absorbed form."""
+        dev = self.device
+        self.plan_host, self.info = mla.mla_decode_plan(self.lens, self.B, self.q_len, self.n_h,
                                                         num_ctas, max_split)
         self.plan_dev = torch.empty(self.plan_host.nbytes, dtype=torch.uint8, device=dev)
         mla.mla_plan_upload(self.plan_host, self.plan_dev, self.plan_dev.numel())
@@ -106,9 +116,6 @@ class DecodeSession(_GraphStep):
         self.o = torch.empty((self.T, self.n_h, D_C), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((self.T, self.n_h), dtype=torch.float32, device=dev)
         self.u = torch.empty((self.T, self.n_h * D_V), dtype=torch.bfloat16, device=dev)
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        if fp8:
-            self._fp8_pool(inp, prefix_layout)
 
     def _fp8_pool(self, inp, layout):
         """The FP8 cache of this workload: every slot starts as a large
@@ -236,7 +243,13 @@ class PrefillSession(_GraphStep):
     The inputs are a DecodeSession's (``inp.w.q_len`` new tokens per sequence), and so is the
     result u, for the queries of the last ``q_lens[b]`` new tokens of each sequence (default:
     all): the same u as the absorbed form's, up to rounding. ``norm``: (weights of the latent's
-    norm as bf16 bits [512] or None, eps). ``layout``: the pairs of k^R and q^R.
+    norm as bf16 bits [512] or None, eps). ``layout``: the pairs of k^R and q^R. Any number of new
+    tokens and 1..128 heads.
+
+    A decode step over a cache that has normed latents or the half layout goes through the
+    library's calls: DecodeSession appends without the norm and turns interleaved pairs. The new
+    token enters through mla_norm_append[_fp8] with the same norm and layout, mla_rope_heads turns
+    q^R, and mla_absorb_q with ``pos`` NULL takes it as it is.
     """
 
     def __init__(self, inp, device="cuda", scale: float = DEFAULT_SCALE,
@@ -245,9 +258,11 @@ class PrefillSession(_GraphStep):
         w = inp.w
         if norm is None and layout != mla.MLA_ROPE_INTERLEAVED:
             raise ValueError("the plain append takes the interleaved layout only")
-        # the decode step's buffers that a chunk shares: cache, table, weights, new rows
+        # the decode step's buffers that a chunk shares: cache, table, weights, new rows (and
+        # its plan where it has one: it takes fewer head counts and shorter chunks)
         self.base = DecodeSession(inp, device, max_split=1, scale=scale, rope_table=rope_table,
-                                  fp8=fp8, prefix_layout=layout)
+                                  fp8=fp8, prefix_layout=layout,
+                                  decode=w.n_h % 16 == 0 and w.q_len <= mla.MAX_Q_LEN)
         b, dev, n_h = self.base, self.base.device, self.base.n_h
         self.w, self.device, self.fp8, self.scale, self.layout = w, dev, fp8, scale, layout
         self.B, self.n_h, self.status = b.B, n_h, b.status

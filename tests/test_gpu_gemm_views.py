@@ -50,3 +50,25 @@ def test_gemm_into_a_column_slice(dev, m, n, k, fp32, workspace):
     want = x @ w.T
     tol = k * 2.0 ** -24 * (x.abs() @ w.abs().T) + (0 if fp32 else 2.0 ** -8) * want.abs()
     assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("m", [63, 64, 129])
+@pytest.mark.parametrize("n,k", [(2112, 2048), (2112, 2064), (264, 64), (20, 2048)])
+def test_gemm_forms_agree_at_their_borders(dev, m, n, k):
+    # 64 tokens and K = 2048 are where bf16 outputs change their form, 8 columns what it
+    # needs: the float32 sums, each rounded once, are the same in every form
+    g = torch.Generator().manual_seed(m + n + k)
+    x = torch.randn(m, k, generator=g).to(torch.bfloat16).to(dev)
+    w = torch.randn(n, k, generator=g).to(torch.bfloat16).to(dev)
+    ld = (n + 7) // 8 * 8
+    c = torch.full((m, ld), 7.0, dtype=torch.bfloat16, device=dev)
+    mla.mla_gemm_bf16(x, k, w, k, c, ld, 0, m, n, k)
+    one = torch.full((m, ld), 7.0, dtype=torch.bfloat16, device=dev)
+    for t in range(m):       # one token at a time: the weights' side
+        mla.mla_gemm_bf16(x[t:], k, w, k, one[t:], ld, 0, 1, n, k)
+    torch.cuda.synchronize()
+    assert torch.equal(c, one) and (c[:, n:] == 7.0).all()
+    xd, wd = x.cpu().double(), w.cpu().double()
+    want = xd @ wd.T
+    tol = k * 2.0 ** -24 * (xd.abs() @ wd.abs().T) + 2.0 ** -8 * want.abs()
+    assert ((c[:, :n].cpu().double() - want).abs() <= tol).all()

@@ -26,8 +26,8 @@
 // load waits for nothing but the tile before the last.
 //
 // Warps (384 threads): 0 TMA, 1 MMA issue and tensor memory, 2 zeroes the
-// values behind a sequence's last key, 4-7 and 8-11 softmax and epilogue of
-// stream 0 and 1 (thread = query row = TMEM lane).
+// values behind a sequence's last key, 3 watches the others, 4-7 and 8-11 softmax
+// and epilogue of stream 0 and 1 (thread = query row = TMEM lane).
 // A ring of eight 16 KB stages carries the tiles in the order they are used:
 // three 64-column chunks of the keys (k^C twice, k^R), two 64-key halves of
 // the values; a barrier each for a tile's keys and its values. The MMAs of one
@@ -46,11 +46,13 @@
 // lies behind a sequence's keys never matters. A row that sees no key gets
 // o = 0 and lse = -inf.
 //
-// Every wait is bounded: it gives up when nothing in the CTA has moved on for about
-// a second (each role counts the items it comes to, the MMA thread its steps too), so
-// the length of a call does not matter: the warp that zeroes tails may wait for its
-// first tile as long as the CTA works. On expiry MLA_DEV_TIMEOUT is set, the CTA stops
-// issuing, lets what it issued land and leaves.
+// Every wait is bounded: warp 3 watches the others (the MMA thread counts its steps, each
+// role the items that have none for it) until they are done. When nothing has moved on for
+// about a second it sets MLA_DEV_TIMEOUT and tells the waiting warps to give up: the CTA
+// stops issuing, lets what it issued land and leaves. The length of a call does not
+// matter: the warp that zeroes tails may wait for its first tile as long as the CTA
+// works. (A clock in each wait is more code at every one of them: 8 short prompts of 16
+// heads 12.4-12.8 us instead of 12.3.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -64,7 +66,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 384;
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kTailWarp = 2;   // 3: idle
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kTailWarp = 2, kWatchWarp = 3;
 // The softmax threads hold a row of a tile; the other warpgroup's registers go to
 // them: 256 x 208 + 128 x 88 = 384 x 168, what the block is launched with.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -88,12 +90,13 @@ enum {
   B_LANDED,                     // values that need zeroing have landed
   B_TAIL,                       // ... and are zeroed
   B_FINAL,
+  B_DONE,                       // the other warps have ended (11 arrivals)
   B_COUNT
 };
 constexpr uint32_t kOffTmemPtr = kOffBar + 8 * B_COUNT;
 constexpr uint32_t kOffAbort = kOffTmemPtr + 4;
-constexpr uint32_t kOffMoved = kOffAbort + 4;        // steps and items that the roles came to
-constexpr uint32_t kOffSwap = (kOffMoved + 4 + 15) & ~15u;   // [stream][128] (maximum, sum)
+constexpr uint32_t kOffMoved = kOffAbort + 4;        // items passed without MMAs; MMA steps
+constexpr uint32_t kOffSwap = (kOffMoved + 8 + 15) & ~15u;   // [stream][128] (maximum, sum)
 constexpr uint32_t kSmemBytes = kOffSwap + 2 * 128 * 8;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -118,34 +121,73 @@ struct Args {
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 
+constexpr uint32_t kStepsDone = 0xFFFFFFFFu;
+
 struct Ctx {
   uint32_t bar_base;
   volatile int *abort_flag;
-  volatile int *moved;
+  uint32_t moved;       // kOffMoved
   uint32_t *status;
   uint64_t wait_ns;
   __device__ uint32_t bar(int i) const { return bar_base + 8u * i; }
-  // One thread of a role: it has come to its next item or step.
-  __device__ __forceinline__ void move() const { atomicAdd(const_cast<int *>(moved), 1); }
+  // One thread of a role: it comes to an item that has no MMA for it.
+  __device__ __forceinline__ void pass_item() const {
+    asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(moved) : "memory");
+  }
+  // The MMA thread: its next step, or the last (kStepsDone).
+  __device__ __forceinline__ void step(uint32_t n) const {
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(moved + 4), "r"(n) : "memory");
+  }
+  __device__ __forceinline__ bool steps_done() const {
+    uint32_t steps;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(steps) : "r"(moved + 4) : "memory");
+    return steps == kStepsDone;
+  }
+  __device__ __forceinline__ uint32_t progress() const {
+    uint32_t items, steps;
+    asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(items), "=r"(steps)
+                 : "r"(moved)
+                 : "memory");
+    return items + steps;
+  }
 };
 
 // (Inlined: a call would have to save the tile's scores around it.)
-__device__ __forceinline__ bool wait_slow(const Ctx &c, uint32_t bar, uint32_t parity, bool drain) {
-  uint64_t t0 = globaltimer_ns();
-  int seen = *c.moved;
+__device__ __forceinline__ bool wait_slow(const Ctx &c, uint32_t bar, uint32_t parity) {
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 0) {
-      if (!drain && *c.abort_flag) return false;
-      const int now = *c.moved;
-      if (now != seen) {
-        seen = now;
-        t0 = globaltimer_ns();
-      } else if (globaltimer_ns() - t0 > c.wait_ns) {
-        *c.abort_flag = 1;
-        report(c.status, MLA_DEV_TIMEOUT);
-        return false;
-      }
+    if ((it & 63) == 0 && *c.abort_flag) return false;
+  }
+}
+
+// What has been issued lands, also after the others have given up.
+__device__ __forceinline__ void drain(const Ctx &c, uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > c.wait_ns) {
+      *c.abort_flag = 1;
+      report(c.status, MLA_DEV_TIMEOUT);
+      return;
+    }
+}
+
+// The watching thread: returns when the other warps have ended or, having told them,
+// when nothing has moved on for too long. It sleeps until the MMAs are done, since its
+// looks cost large calls 5 % otherwise, and is then there when the others end.
+__device__ __forceinline__ void watch(const Ctx &c, uint32_t bar) {
+  uint64_t t0 = globaltimer_ns();
+  uint32_t seen = c.progress();
+  while (!mbar_try_wait(bar, 0)) {
+    if (!c.steps_done()) __nanosleep(200);
+    const uint32_t now = c.progress();
+    if (now != seen) {
+      seen = now;
+      t0 = globaltimer_ns();
+    } else if (globaltimer_ns() - t0 > c.wait_ns) {
+      *c.abort_flag = 1;
+      report(c.status, MLA_DEV_TIMEOUT);
+      return;
     }
   }
 }
@@ -153,12 +195,12 @@ __device__ __forceinline__ bool wait_slow(const Ctx &c, uint32_t bar, uint32_t p
 // Whole warp; false when the wait ran out or another warp has given up.
 __device__ __forceinline__ bool wait_warp(const Ctx &c, uint32_t bar, uint32_t parity) {
   bool ok = mbar_try_wait(bar, parity);
-  if (!ok) ok = wait_slow(c, bar, parity, false);
+  if (!ok) ok = wait_slow(c, bar, parity);
   return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ bool wait_one(const Ctx &c, uint32_t bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || wait_slow(c, bar, parity, false);
+  return wait_slow(c, bar, parity);
 }
 
 // D[tmem] (+)= A[tmem] * B[smem desc], bf16 inputs, fp32 accumulate.
@@ -364,15 +406,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
   Ctx ctx;
   ctx.bar_base = base + kOffBar;
   ctx.abort_flag = reinterpret_cast<volatile int *>(smem + kOffAbort);
-  ctx.moved = reinterpret_cast<volatile int *>(smem + kOffMoved);
+  ctx.moved = base + kOffMoved;
+  static_assert(kOffMoved % 8 == 0, "two words read at once");
   ctx.status = a.status;
   ctx.wait_ns = a.wait_ns;
   static_assert(B_COUNT <= 32, "a lane per barrier");
   if (warp == kTmaWarp) {
-    if (lane == 0) *ctx.abort_flag = *ctx.moved = 0;
+    if (lane == 0) *ctx.abort_flag = 0;
+    if (lane < 2) reinterpret_cast<volatile int *>(smem + kOffMoved)[lane] = 0;
     if (lane < B_COUNT)
       mbar_init(ctx.bar(lane),
-                lane >= B_PFULL && lane < B_PFULL + 4 ? 4 : lane == B_SWAP ? 8 : 1);
+                lane >= B_PFULL && lane < B_PFULL + 4 ? 4
+                : lane == B_SWAP                    ? 8
+                : lane == B_DONE                    ? kThreads / 32 - 1
+                                                    : 1);
     fence_mbar_init_cluster();
   }
   if (warp == kMmaWarp) tmem_alloc(base + kOffTmemPtr, 512);
@@ -438,12 +485,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
       bool turns = false;             // how the shared memory is laid out
       for (int i = i0; i < i1 && ok; ++i) {
         const Item it = load_item<kTurns>(a, items + i);
-        ctx.move();
-        if (!it.ok) {
-          report(a.status, MLA_DEV_BAD_PLAN);
+        if (!it.ok || it.tiles == 0) {
+          if (!it.ok) report(a.status, MLA_DEV_BAD_PLAN);
+          ctx.pass_item();
           continue;
         }
-        if (it.tiles == 0) continue;
         const int row0 = it.k_row + it.tile_begin * kPrefillKeys;
         if (kTurns && it.turns != turns) {
           // the layouts overlap: everything of the last item is used first
@@ -483,10 +529,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
       }
       // what was issued lands before the CTA leaves
       for (uint32_t b = 0; b < 2; ++b) {
-        if (keys > b) wait_slow(ctx, ctx.bar(B_KFULL + b), ((keys - 1 - b) >> 1) & 1, true);
-        if (values > b) wait_slow(ctx, ctx.bar(B_VFULL + b), ((values - 1 - b) >> 1) & 1, true);
-        if (nq[b] > 0) wait_slow(ctx, ctx.bar(B_QFULL + b), (nq[b] - 1) & 1, true);
+        if (keys > b) drain(ctx, ctx.bar(B_KFULL + b), ((keys - 1 - b) >> 1) & 1);
+        if (values > b) drain(ctx, ctx.bar(B_VFULL + b), ((values - 1 - b) >> 1) & 1);
+        if (nq[b] > 0) drain(ctx, ctx.bar(B_QFULL + b), (nq[b] - 1) & 1);
       }
+      mbar_arrive(ctx.bar(B_DONE));
     }
   } else if (warp == kMmaWarp) {
     // One thread waits and issues. The softmax warps leave it few issue slots,
@@ -500,12 +547,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
       const uint64_t v_desc = smem_desc(ring, kChunk / 2, 1024, kSwizzle128B);
       uint32_t n = 0;                 // tiles of the items before this one
       // phases waited for, a bit per stream: queries, probabilities
-      uint32_t nq = 0, np = 0, tails = 0;
+      uint32_t nq = 0, np = 0, tails = 0, steps = 0;
       bool ok = true;
       for (int i = i0; i < i1 && ok; ++i) {
         const Item it = load_item<kTurns>(a, items + i);
-        ctx.move();
-        if (!it.ok || it.tiles == 0) continue;
+        if (!it.ok || it.tiles == 0) {
+          ctx.pass_item();
+          continue;
+        }
         const int n0 = it.count[0], n1 = it.count[1];   // no turns: n1 is 0 or >= n0
         const bool turns = kTurns && it.turns;
         // Step j of stream q: its output j, then its scores j + 1 (one piece of code
@@ -516,7 +565,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
 #pragma unroll 1
           for (int q = 0; q < 2 && ok; ++q) {
             const int count = q ? n1 : n0;
-            ctx.move();
+            ctx.step(++steps);
             if (j >= 0 && j < count) {
               const int t = turns ? 2 * j + q : j;
               const uint32_t k = n + t;
@@ -581,7 +630,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
         n += it.tiles;
       }
       mma_commit(ctx.bar(B_FINAL));
-      wait_slow(ctx, ctx.bar(B_FINAL), 0, true);
+      drain(ctx, ctx.bar(B_FINAL), 0);
+      ctx.step(kStepsDone);
+      mbar_arrive(ctx.bar(B_DONE));
     }
     __syncwarp();
   } else if (warp == kTailWarp) {
@@ -592,8 +643,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
     uint32_t n = 0, tails = 0;
     for (int i = i0; i < i1; ++i) {
       const Item it = load_item<kTurns>(a, items + i);
-      if (lane == 0) ctx.move();
-      if (!it.ok || it.tiles == 0) continue;
+      if (!it.ok || it.tiles == 0) {
+        if (lane == 0) ctx.pass_item();
+        continue;
+      }
       const int t = it.tiles - 1;
       if (it.tail(t)) {
         if (!wait_warp(ctx, ctx.bar(B_LANDED), tails++ & 1)) break;
@@ -614,6 +667,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
       }
       n += it.tiles;
     }
+    if (lane == 0) mbar_arrive(ctx.bar(B_DONE));
+  } else if (warp == kWatchWarp) {
+    if (lane == 0) watch(ctx, ctx.bar(B_DONE));
   } else if (warp >= 4) {
     regs_inc<kSoftmaxRegs>();
     // softmax and epilogue: thread = query row of the stream
@@ -628,7 +684,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
     bool ok = true, unread = false;
     for (int i = i0; i < i1 && ok; ++i) {
       const Item it = load_item<kTurns>(a, items + i);
-      if (lane == 0) ctx.move();
+      if ((!it.ok || it.count[q] == 0) && lane == 0) ctx.pass_item();
       if (!it.ok) continue;
       const int row = lrow + (kTurns && it.turns ? 0 : 128 * q);   // of the item
       const bool has = row < it.q_rows;
@@ -810,6 +866,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant_
           a.lse[out_row * a.n_h + it.h] = lse;
       }
     }
+    if (lane == 0) mbar_arrive(ctx.bar(B_DONE));
   }
   tc_fence_before();
   __syncthreads();

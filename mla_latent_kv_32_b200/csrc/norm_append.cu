@@ -9,8 +9,8 @@
 // side (when there is one) is the neighbouring warp, so that the two halves of
 // a fused down-projection's row are read together. A lane issues all 16-byte
 // loads of its row before it uses the first. Bound: HBM for many tokens (16381
-// with q_dim 1536, 142.6 MB: 25.0 us, 5.7 TB/s), the launch and three dependent
-// memory round trips (position, page id, store) for few (64: 2.0 us).
+// with q_dim 1536, 142.6 MB: 25.6 us, 5.6 TB/s), the launch and three dependent
+// memory round trips (position, page id, store) for few (64: 1.9 us).
 // Sums of squares, the mean and the scaled values are float32; each output is
 // rounded once (bf16 nearest even, or E4M3 of the float32 value).
 #include "internal.h"
@@ -282,7 +282,7 @@ mla_status_t launch_norm_append(const NormAppendArgs &a, cudaStream_t stream) {
   const long long warps = (long long)a.n_tokens * (a.q_dim > 0 ? 2 : 1);
   const unsigned grid = (unsigned)((warps + kWarpsPerCta - 1) / kWarpsPerCta);
   // One wave even with few resident warps: the shorter chain (64 tokens with
-  // q_dim 1536: 2.0 against 3.3 us); else more warps (16381: 25.5 against 34.8).
+  // q_dim 1536: 1.9 against 3.1 us); else more warps (16381: 25.6 against 30.3).
   int sms = 0;
   mla_status_t st = device_info(&sms, nullptr, nullptr);
   if (st != MLA_OK) return st;

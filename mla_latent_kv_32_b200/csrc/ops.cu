@@ -40,8 +40,10 @@ constexpr int kGridTokens = 65535 * 128;   // tokens on the grid's y axis
 // A short reduction, where the stores of C are most of the time: the tokens are
 // the M side and a thread's output row is contiguous (wide stores). The same
 // bits; 16384 tokens x 16384 x 512: 313 us against 1031 the other way round, 256
-// x 16384 x 512: 12 against 41; but 4096 x 7168 x 16384: 888 against 815 (with
-// 16-byte stores, 10 % slower on the short ones). (Fewer than 64 tokens fill
+// x 16384 x 512: 9 against 41; but 4096 x 7168 x 16384: 888 against 815 (with
+// 16-byte stores, 10 % slower on the short ones), 2048 x 7168 x 16384 468 against 451.
+// Between 2048 and 16384 the rows are still ahead (16384 x 2112 x 7168: 436 against
+// 538), but the limit is where it was measured first. (Fewer than 64 tokens fill
 // little of a tile's 128 rows and stay on the N side.)
 bool projection_by_rows(int M, int N, int K, bool c_fp32, bool workspace) {
   return !c_fp32 && !workspace && M >= kManyTokens && M <= kGridTokens && K <= kShortK &&

@@ -9,8 +9,9 @@
 // token: the 16 table values are read once for them, and all its loads are in
 // flight together. Neighbouring threads own neighbouring pieces, then
 // neighbouring heads, so a warp's accesses are contiguous where the rows are.
-// Bound: HBM for many tokens (4099 x 128 heads of 64: 22.5 us, 6.0 TB/s, a plain
-// copy of as many bytes takes 22.9), the launch for few (64 x 128 heads: 2.2 us).
+// Bound: HBM for many tokens (4099 x 128 heads of 64: 23.0 us, 5.9 TB/s, an
+// elementwise pass over as many bytes takes 21.7), the launch for few (64 x 128 heads:
+// 2.2 us).
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -20,7 +21,9 @@ namespace {
 using sm100::cvt_bf16x2;
 
 constexpr int kThreads = 128;
-constexpr int kHeads = 4;   // heads per thread: 1, 2, 4 take 27.0, 24.1, 22.5 us on 4099 x 128 heads
+// heads per thread: 1, 2, 4 take 27.0, 24.1, 22.5 us on 4099 x 128 heads in one sweep,
+// 26.5, 22.3, 23.0 in another
+constexpr int kHeads = 4;
 
 __device__ __forceinline__ void turn8(const uint4 &a, const uint4 &b, const float4 (&cs)[4],
                                       bool half, uint4 &oa, uint4 &ob) {

@@ -72,3 +72,29 @@ def test_gemm_forms_agree_at_their_borders(dev, m, n, k):
     want = xd @ wd.T
     tol = k * 2.0 ** -24 * (xd.abs() @ wd.abs().T) + 2.0 ** -8 * want.abs()
     assert ((c[:, :n].cpu().double() - want).abs() <= tol).all()
+
+
+def test_split_output_in_a_column_slice_captured(dev):
+    # the clear of the slice is part of a captured call, and of every replay
+    m, n, k, ld = 5, 64, 4096, 128
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(m, k, generator=g).to(torch.bfloat16).to(dev)
+    w = torch.randn(n, k, generator=g).to(torch.bfloat16).to(dev)
+    assert mla.mla_debug_projection_plan(m, n, k, 1, 0)["splits"] > 1
+    buf = torch.full((m, ld), 7.0, dtype=torch.float32, device=dev)
+    call = lambda s: mla.mla_gemm_bf16(x, k, w, k, buf[:, 32:], ld, 1, m, n, k, s)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(side)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    got = buf.cpu()
+    xd, wd = x.cpu().double(), w.cpu().double()
+    tol = k * 2.0 ** -24 * (xd.abs() @ wd.abs().T)
+    assert ((got[:, 32:96].double() - xd @ wd.T).abs() <= tol).all()
+    assert (got[:, :32] == 7.0).all() and (got[:, 96:] == 7.0).all()
